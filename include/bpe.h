@@ -410,7 +410,7 @@ typedef enum {
      h = x + residual                          (residual NULL: h = x)
      y = h * weight / sqrt(mean(h^2) + eps)
      s = max(max|y| / 448, 2^-126)             for each block of 128 columns
-     q = y / s in e4m3, to the nearest, ties to even
+     q = y / s, the f32 quotient, in e4m3 to the nearest, ties to even
    x, residual, weight and sum have the given type; sums are f32 (the mean's
    f64), and y is formed from h before it is rounded. The last block may be
    shorter. A block with a value that is no number (NaN in x, residual or
@@ -426,7 +426,7 @@ bpe_status bpe_norm_quant(const void *x, size_t x_stride, const void *residual, 
                           size_t sum_stride, uint8_t *q, size_t q_stride, float *scales, void *stream);
 
 /* A weight matrix w [n, k] in e4m3 with one scale for each block of 128 x 128
-   (made as by bpe_norm_quant, from the block's largest magnitude): done once
+   (s and q as in bpe_norm_quant, from the block's largest magnitude): done once
    when weights are loaded. scales: ceil(n / 128) x ceil(k / 128), without
    gaps. Errors: BPE_EINVAL, BPE_EHIP. */
 #define BPE_PRODUCT_MAX 0x7FFF80u   /* largest m, n and k (65,535 blocks of 128) */

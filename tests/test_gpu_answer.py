@@ -240,6 +240,37 @@ def test_quant_weight(bpe, dtype, n, k):
     assert np.all(off <= (2.0 ** -4 * np.abs(y) + 2.0 ** -10 * sw) * (1 + 2.0 ** -18))
 
 
+def _by_division(y, s):
+    """e4m3 codes of the f32 quotients y / s."""
+    return torch.from_numpy(y.float().cpu().numpy() / s.astype(np.float32)).to(E4M3)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quant_weight_divides(bpe, dtype):
+    """Values of 8 to 12 bits often lie half way between two codes of their
+    block's scale: the quotient has to be rounded once."""
+    n, k = 515, 1030
+    w = _randn(7, n, k) * 0.02
+    w[130:300] *= torch.exp2(-135 * torch.rand(170, 1, generator=torch.Generator().manual_seed(1)))
+    w[300:, :500] *= 1e37
+    w[5, 100:200] = torch.tensor([0.0, -0.0] * 50)
+    w = w.clamp(-torch.finfo(dtype).max, torch.finfo(dtype).max).to(dtype)
+    q, s = bpe.quant_weight(w.cuda())
+    assert _same(q, _by_division(w, answers.spread(s.cpu().numpy(), n, k, True)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [500, 1024, 2000, 4096, 8192, 65536])
+def test_norm_quant_divides(bpe, dtype, d):
+    """Rows of 1 and -1 have a norm of exactly 1, so that y is the weight."""
+    sign = torch.sign(_randn(d, 3, d)).to(dtype)
+    w = (1 + 0.3 * _randn(d + 1, d)).to(dtype)
+    w[7:9] = torch.tensor([0.0, -0.0])
+    w[256:400] *= 2.0 ** -120 if dtype != torch.float16 else 2.0 ** -14
+    q, s, _ = bpe.norm_quant(sign.cuda(), w.cuda(), eps=0.0)
+    assert _same(q, _by_division(sign * w, answers.spread(s.cpu().numpy(), 3, d, False)))
+
+
 # ---------------------------------------------------------------- sampling
 
 def _check_sample(ids, logp, x, u, settings):
