@@ -50,7 +50,7 @@ __device__ __forceinline__ float scale_of(uint32_t max_bits) {
 // lie half way between two codes, where the product alone falls to either side
 // (one of 2,000 bfloat16 weights came out a code off). The division itself for
 // each would cost 16,384 x 8,192 rows 182 us instead of 174, and 2,000 x 20,000
-// 180 instead of 153.
+// 180 instead of 142.
 __device__ __forceinline__ void divide(float (&v)[8], float s) {
     if (s < 0x1p-90f) {  // remainders of such numbers could leave the range of f32
 #pragma unroll
@@ -124,7 +124,15 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_norm_quant(
 #pragma unroll
         for (int i = 0; i < WAVES; ++i) squares += s_sum[i];
     }
-    const float inv_rms = (float)(1.0 / sqrt(squares / (double)d + (double)eps));
+    const double inv = 1.0 / sqrt(squares / (double)d + (double)eps);
+    float inv_rms = (float)inv;
+    if (inv > 0x1p100) {  // only with an eps of 0: past the range of f32, where the row itself is as near to zero
+        inv_rms = (float)(inv * 0x1p-64);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[j][i] *= 0x1p64f;
+    }
     const uint32_t blocks = (d + NQ_BLOCK - 1u) / NQ_BLOCK;
     q += row * qs;
     scales += (size_t)row * blocks;

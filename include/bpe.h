@@ -414,7 +414,8 @@ typedef enum {
    x, residual, weight and sum have the given type; sums are f32 (the mean's
    f64), and y is formed from h before it is rounded. The last block may be
    shorter. A block with a value that is no number (NaN in x, residual or
-   weight, an infinite h) has no number as its scale or in q.
+   weight, an infinite h, zeros alone with an eps of 0) has no number as its
+   scale or in q.
      sum     out, or NULL: h. May be x or residual itself (same stride)
      q       out, rows x d
      scales  out, rows x ceil(d / 128), without gaps

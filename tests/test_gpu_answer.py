@@ -106,6 +106,25 @@ def test_norm_quant_of_zeros_extremes_and_no_numbers(bpe):
     assert np.isnan(s[0]).tolist() == [False, True, False] and np.isnan(q[0, 128:256]).all() and not np.isnan(q[0, 256:]).any()
 
 
+@pytest.mark.parametrize("d", [40, 700, 3000, 20001])
+def test_norm_quant_of_tiny_rows_without_eps(bpe, d):
+    """Root mean squares from the smallest f32 numbers on: y is of the
+    weight's size all the same."""
+    w = (1 + 0.3 * _randn(d, d)).cuda()
+    x = _randn(d + 1, 6, d) * torch.tensor([2.0 ** -149, 2.0 ** -140, 2.0 ** -128, 2.0 ** -126, 2.0 ** -100, 1.0])[:, None].double()
+    x = x.float()
+    x[0] = 0.0
+    x[0, d // 2] = 2.0 ** -149
+    _check_norm(*bpe.norm_quant(x.cuda(), w, eps=0.0), x, None, w, 0.0)
+    x = x.bfloat16()
+    x[0, d // 3] = 2.0 ** -133
+    q, s, h = (t.cpu() for t in bpe.norm_quant(x.cuda(), w.bfloat16(), eps=0.0))
+    some = (x != 0).any(1)  # the second row's numbers are too small for bfloat16: 0 / 0
+    assert some.tolist() == [True, False, True, True, True, True]
+    _check_norm(q[some], s[some], h[some], x[some], None, w.bfloat16(), 0.0)
+    assert bool(q[1].float().isnan().all()) and bool(s[1].isnan().all()) and not bool(h[1].any())
+
+
 # ---------------------------------------------------------------- product
 
 def _operand(seed, rows, k, rows_too):
