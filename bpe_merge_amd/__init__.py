@@ -651,7 +651,13 @@ def matmul_scaled(a, a_scales, b, b_scales, out_dtype=None, out=None):
     float8_e4m3fn, with a's scales for each row's 128 columns and b's for
     each 128 x 128 block (as norm_quant and quant_weight give them). Returns
     [..., n] in out_dtype (bfloat16 if not given), written to out if given (a
-    tensor of that shape with adjacent columns)."""
+    tensor of that shape with adjacent columns).
+
+    float32 and float16 results, and all of up to 64 rows of a, have f32 sums.
+    bfloat16 results of more rows may lose up to 7 * 2^-13 of the largest of
+    every 8 neighbouring products. A row's last bits go by the number of rows
+    and its place among them. An operand whose columns are not adjacent (a
+    transposed b) is copied on every call."""
     torch = _torch()
     _cuda(a, "a", torch.float8_e4m3fn)
     _cuda(b, "b", torch.float8_e4m3fn)

@@ -252,9 +252,9 @@ void launch_streams(const bpek::Product& p, hipStream_t s) {
 // in us): 256 x 256, one to a CU, 2.1; 256 x 128, one to a CU, 1.15; 128 x
 // 128, 0.85 alone on a CU and 1.55 for two. On 2,048 x 65,536 x 4,096 they
 // take 534, 620 and 775 us; on 1,024 x 8,192 x 8,192, where the widest leave
-// half of the CUs idle, 106, 66 and 78 us. Exact sums (f32 results) take 1.6
-// times as long in each, and have no 256 x 256, whose registers do not hold
-// their fragments (nor anything but full blocks); 128 x 128 alone on a CU
+// half of the CUs idle, 106, 66 and 78 us. Exact sums (f32 and binary16 results)
+// take 1.6 times as long in each, and have no 256 x 256, whose registers do not
+// hold their fragments (nor anything but full blocks); 128 x 128 alone on a CU
 // then takes 8 waves (128 x 32,256 x 4,096: 41 against 54 us). Pieces that go
 // through registers take the last (700 x 32,256 x 3,909: 215 us, 235 in the
 // second; 142 where rows are whole pieces). Where even of the last there are
@@ -262,7 +262,7 @@ void launch_streams(const bpek::Product& p, hipStream_t s) {
 // 8,192: 66 against 11 us; 1,000 x 456 x 8,191: 86 against 64).
 template <typename T, bpek::Pieces KIND>
 void launch_tiles(const bpek::Product& p, hipStream_t s) {
-    constexpr bool EXACT = std::is_same_v<T, bpek::F32>, COPIED = bpek::copied(KIND);
+    constexpr bool EXACT = !std::is_same_v<T, bpek::BF16>, COPIED = bpek::copied(KIND);
     constexpr uint64_t CUS = 256;
     auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
     auto tiles = [&](uint64_t bn, uint64_t bm) { return up(p.n, bn) * up(p.m, bm); };

@@ -8,14 +8,18 @@
 // f32. The inner sum itself has two forms:
 //   e4m3 MFMA, one 16 x 16 x 128 instruction. Measured: of every 8
 //     neighbouring products it drops what lies below 2^-13 of the largest
-//     one's power of two; sums across these groups are f32. On normal data
-//     that is 1.5e-5 of the result's norm, a hundredth of what rounding to
-//     bfloat16 (a tenth of what rounding to binary16) costs.
+//     one's power of two; sums across these groups are f32. So a group is off
+//     by less than 7 * 2^-13 of its largest product: below half a bfloat16 step
+//     (2^-8) of that product, but more than a binary16 one's (2^-11), and all
+//     of the result where the large products cancel. On normal data that is
+//     1.5e-5 of the result's norm.
 //   f16 MFMA, four 16 x 16 x 32 instructions on operands widened in
 //     registers: e4m3 values are f16 values, their products are exact and
 //     all sums f32. Half the matrix rate, and 16 conversions a fragment.
-// Few rows are bound by reading b, where the exact form costs nothing; many
-// rows take it for f32 results, and the e4m3 form for 16-bit ones.
+// Few rows are bound by reading b, where the exact form costs nothing. Many
+// rows take it for f32 and binary16 results; bfloat16 ones take the e4m3 form,
+// for its rate (2,048 x 65,536 x 4,096: 534 us against 960 in
+// binary16), and callers who want f32 sums there ask for f32 results.
 // b's rows are the MFMA's first operand and a's its second, so a lane of the
 // result holds one row m and four neighbouring n: one scale factor per lane
 // and tile, and vector stores.

@@ -437,9 +437,16 @@ bpe_status bpe_quant_weight(const void *w, size_t w_stride, bpe_type type, size_
 /* out[i, j] = sum over blocks c of 128 columns of
      a_scales[i, c] * b_scales[j / 128, c] * (sum over the block of a[i, .] * b[j, .])
    for a [m, k] (rows of bpe_norm_quant) and b [n, k] (of bpe_quant_weight),
-   both e4m3, with f32 sums, rounded once to out_type. Any k and any strides;
-   fastest where k is a multiple of 128 and a, b and their strides are
-   multiples of 16 bytes. Results do not depend on other rows' values or on
+   both e4m3. Any k and any strides; fastest where k is a multiple of 128 and a,
+   b and their strides are multiples of 16 bytes.
+   Sums are f32, rounded once to out_type, but for BPE_BFLOAT with m above 64:
+   there every 8 neighbouring columns may lose up to 7 * 2^-13 of their largest
+   product before the sums. That is less than half a bfloat16 step of this
+   product, but can be all of a result whose large products cancel; BPE_FLOAT
+   and BPE_HALF have f32 sums for every m.
+   The order of sums, and with it a result's last bits, goes by m, n, k, the
+   type, the alignment, and by a row's place in a and in b: equal rows of one
+   call need not give equal results. They do not depend on other rows' values or on
    scheduling. Errors: BPE_EINVAL (k of 0, sizes above BPE_PRODUCT_MAX, a
    stride below its row, host memory, arrays on different devices), BPE_EHIP. */
 bpe_status bpe_matmul_scaled(const uint8_t *a, size_t a_stride, const float *a_scales, size_t a_scales_stride,

@@ -193,6 +193,29 @@ def test_matmul_scaled_of_every_tile(bpe, m, n, k):
         assert np.all(np.abs(got - want) <= tol * (1 + 2.0 ** -8))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m, n, k", [(16, 40, 128), (64, 6200, 256), (65, 300, 128), (130, 300, 272), (130, 300, 257),
+                                     (600, 8256, 1024), (520, 16640, 384), (789, 9244, 128), (130, 456, 2048)])
+def test_matmul_scaled_of_sums_that_cancel(bpe, dtype, m, n, k):
+    """Two of the groups of 8 columns hold one product of 2^16 and seven of
+    7.5, just below 2^-13 of it; the large ones cancel. f32 sums leave 105;
+    bfloat16 results of more than 64 rows are allowed to lose the small ones."""
+    row = torch.zeros(2, k)
+    for at, large in ((0, 256.0), (64, -256.0)):
+        row[0, at:at + 8], row[1, at:at + 8] = 2.0, 3.75
+        row[0, at + 3], row[1, at + 3] = 256.0, large
+    a, b = row[:1].expand(m, k).to(E4M3).contiguous(), row[1:].expand(n, k).to(E4M3).contiguous()
+    blocks = -(-k // 128)
+    sa, sb = torch.ones(m, blocks), torch.ones(-(-n // 128), blocks)
+    out = bpe.matmul_scaled(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), out_dtype=dtype).double()
+    want, size = answers.product(a[:1], sa[:1], b[:1], sb[:1])
+    assert want[0, 0] == 105.0
+    tol = answers.product_tolerance(size, blocks) + answers.half_step(dtype) * want
+    if dtype == torch.bfloat16 and m > 64:
+        tol += answers.product_dropped(a[:1], sa[:1], b[:1], sb[:1])
+    assert float((out - 105.0).abs().max()) <= tol[0, 0] * (1 + 2.0 ** -8)
+
+
 @pytest.mark.parametrize("m, n, k, pad", [(3, 50, 256, 16), (3, 50, 256, 3), (40, 100, 384, 16), (40, 100, 384, 1), (150, 140, 256, 48),
                                           (150, 140, 256, 5), (3, 50, 90, 7), (70, 7000, 2064, 1),
                                           (3, 9000, 6800, 1)])
