@@ -15,6 +15,7 @@
 #include "host.hpp"
 #include "decode.hpp"
 #include "norm.hpp"
+#include "plan.hpp"
 #include "product.hpp"
 #include "sample.hpp"
 
@@ -155,22 +156,26 @@ bpe_status bpe_norm_quant(const void* x, size_t x_stride, const void* residual, 
     with_type(type, [&](auto tag) {
         using T = decltype(tag);
         using raw = typename T::raw;
-        auto launch = [&](auto kernel, uint32_t grid, uint32_t tpb) {
-            hipLaunchKernelGGL(kernel, dim3(grid), dim3(tpb), 0, s, static_cast<const raw*>(x), x_stride,
-                               static_cast<const raw*>(residual), residual_stride, static_cast<const raw*>(weight),
-                               uint32_t(rows), uint32_t(d), eps, static_cast<raw*>(sum), sum_stride, q, q_stride,
-                               scales);
+        auto launch = [&](auto kernel, uint32_t group_rows, uint32_t tpb) {
+            bpek::in_parts(rows, group_rows, bpek::groups_in_x(tpb), [&](size_t at, uint32_t part, uint32_t groups) {
+                const raw* r = static_cast<const raw*>(residual);
+                raw* h = static_cast<raw*>(sum);
+                hipLaunchKernelGGL(kernel, dim3(groups), dim3(tpb), 0, s, static_cast<const raw*>(x) + at * x_stride, x_stride,
+                                   r ? r + at * residual_stride : r, residual_stride, static_cast<const raw*>(weight), part,
+                                   uint32_t(d), eps, h ? h + at * sum_stride : h, sum_stride, q + at * q_stride, q_stride,
+                                   scales + at * ((d + 127) / 128));
+            });
         };
         // The fewest lanes that hold a row in at most 32 columns each: a wave
         // up to 1,024 columns (4 rows in a workgroup, no barrier), 4 waves up
         // to 8,192 (more lanes with fewer columns would wait for each other's
         // sums more often), 16 waves beyond.
-        if (d <= 512) launch(bpek::k_norm_quant<T, 1, 1>, uint32_t((rows + 3) / 4), 256);
-        else if (d <= 1024) launch(bpek::k_norm_quant<T, 1, 2>, uint32_t((rows + 3) / 4), 256);
-        else if (d <= 2048) launch(bpek::k_norm_quant<T, 4, 1>, uint32_t(rows), 256);
-        else if (d <= 4096) launch(bpek::k_norm_quant<T, 4, 2>, uint32_t(rows), 256);
-        else if (d <= 8192) launch(bpek::k_norm_quant<T, 4, 4>, uint32_t(rows), 256);
-        else launch(bpek::k_norm_quant<T, 16, 8>, uint32_t(rows), 1024);
+        if (d <= 512) launch(bpek::k_norm_quant<T, 1, 1>, 4, 256);
+        else if (d <= 1024) launch(bpek::k_norm_quant<T, 1, 2>, 4, 256);
+        else if (d <= 2048) launch(bpek::k_norm_quant<T, 4, 1>, 1, 256);
+        else if (d <= 4096) launch(bpek::k_norm_quant<T, 4, 2>, 1, 256);
+        else if (d <= 8192) launch(bpek::k_norm_quant<T, 4, 4>, 1, 256);
+        else launch(bpek::k_norm_quant<T, 16, 8>, 1, 1024);
     });
     HIP_TRY(hipGetLastError());
     return BPE_OK;
@@ -429,8 +434,16 @@ bpe_status bpe_sample(const void* logits, size_t stride, bpe_type type, size_t r
     with_type(type, [&](auto tag) {
         using T = decltype(tag);
         auto launch = [&](auto kernel, uint32_t tpb) {
-            hipLaunchKernelGGL(kernel, dim3(uint32_t(rows)), dim3(tpb), 0, static_cast<hipStream_t>(stream),
-                               static_cast<const typename T::raw*>(logits), stride, uint32_t(vocab), u, par, ids, logp);
+            bpek::in_parts(rows, 1, bpek::groups_in_x(tpb), [&](size_t at, uint32_t, uint32_t groups) {
+                bpek::Sampling here = par;
+                if (here.temperatures) here.temperatures += at;
+                if (here.top_ks) here.top_ks += at;
+                if (here.top_ps) here.top_ps += at;
+                if (here.min_ps) here.min_ps += at;
+                hipLaunchKernelGGL(kernel, dim3(groups), dim3(tpb), 0, static_cast<hipStream_t>(stream),
+                                   static_cast<const typename T::raw*>(logits) + at * stride, stride, uint32_t(vocab), u + at,
+                                   here, ids + at, logp ? logp + at : logp);
+            });
         };
         if (vocab <= 2048) launch(bpek::k_sample<T, 256, 4>, 256);
         else if (vocab <= 8192) launch(bpek::k_sample<T, 256, 16>, 256);

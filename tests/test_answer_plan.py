@@ -1,0 +1,66 @@
+"""How calls of the operators between a hidden state and text are cut into
+launches, checked without a device: the arithmetic is host code of its own."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+SOURCE = """
+#include "plan.hpp"
+extern "C" {
+uint64_t groups_in_x(uint64_t threads) { return bpek::groups_in_x(threads); }
+uint64_t groups_in_y() { return bpek::GROUPS_IN_Y; }
+// each part's first row, rows and workgroups; returns how many parts there are
+int parts(uint64_t rows, uint64_t group_rows, uint64_t most_groups, uint64_t *out, int room) {
+    int n = 0;
+    bpek::in_parts(rows, group_rows, most_groups, [&](uint64_t at, uint32_t part, uint32_t groups) {
+        if (n < room) out[3 * n] = at, out[3 * n + 1] = part, out[3 * n + 2] = groups;
+        ++n;
+    });
+    return n;
+}
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    where = tmp_path_factory.mktemp("plan")
+    src, lib = where / "plan.cpp", where / "plan.so"
+    src.write_text(SOURCE)
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
+                           os.path.join(ROOT, "bpe_merge_amd", "csrc"), "-o", str(lib), str(src)])
+    lib = ctypes.CDLL(str(lib))
+    u64 = ctypes.c_uint64
+    lib.groups_in_x.argtypes, lib.groups_in_x.restype, lib.groups_in_y.restype = [u64], u64, u64
+    lib.parts.argtypes = [u64, u64, u64, ctypes.POINTER(u64), ctypes.c_int]
+    return lib
+
+
+def _parts(plan, rows, group_rows, most):
+    room = 600
+    out = (ctypes.c_uint64 * (3 * room))()
+    n = plan.parts(rows, group_rows, most, out, room)
+    assert n <= room
+    return [tuple(out[3 * i:3 * i + 3]) for i in range(n)]
+
+
+# threads of a workgroup and its rows, as norm and sampling launch them
+@pytest.mark.parametrize("threads, group_rows", [(256, 4), (256, 1), (1024, 1)])
+def test_rows_beyond_a_launch_go_in_parts(plan, threads, group_rows):
+    most = plan.groups_in_x(threads)
+    assert most * threads < 1 << 32 <= (most + 1) * threads
+    limit = most * group_rows
+    for rows in (1, 2, group_rows + 1, limit - 1, limit, limit + 1, 2 * limit + 3, 0x7FFFFFFF):
+        parts = _parts(plan, rows, group_rows, most)
+        assert len(parts) == -(-rows // limit)
+        at = 0
+        for first, part, groups in parts:
+            assert first == at and 0 < part <= 0x7FFFFFFF
+            assert (groups - 1) * group_rows < part <= groups * group_rows and groups * threads < 1 << 32
+            at += part
+        assert at == rows
+    assert _parts(plan, 0, group_rows, most) == []

@@ -125,6 +125,20 @@ def test_norm_quant_of_tiny_rows_without_eps(bpe, d):
     assert bool(q[1].float().isnan().all()) and bool(s[1].isnan().all()) and not bool(h[1].any())
 
 
+def test_norm_quant_of_more_rows_than_a_launch_takes(bpe):
+    """2^26 rows of up to 1,024 columns are more threads than a launch has."""
+    rows = (1 << 26) + 5
+    x = torch.randn(rows, 1, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+    w = torch.tensor([1.5]).bfloat16().cuda()
+    q, s, h = bpe.norm_quant(x, w, residual=x, eps=0.5)
+    step = 1 << 24
+    for at in range(0, rows, step):
+        part = slice(at, min(rows, at + step))
+        for got, want in zip((q, s, h), bpe.norm_quant(x[part], w, residual=x[part], eps=0.5)):
+            assert torch.equal(got[part].view(torch.uint8), want.view(torch.uint8))
+    _check_norm(q[-9:], s[-9:], h[-9:], x[-9:], x[-9:], w, 0.5)
+
+
 # ---------------------------------------------------------------- product
 
 def _operand(seed, rows, k, rows_too):
@@ -417,6 +431,30 @@ def test_sample_of_masked_rows(bpe, dtype):
                 _check_sample(ids.cpu(), logp.cpu(), x, u, s)
             else:  # weights nearly all equal: compare what does not hang on their 40th bit
                 _check_sample(ids.cpu()[[0, 1, 10, 11]], logp.cpu()[[0, 1, 10, 11]], x[[0, 1, 10, 11]], u[[0, 1, 10, 11]], s)
+
+
+def test_sample_of_more_rows_than_a_launch_takes(bpe):
+    """2^24 rows in workgroups of 256 threads, each row with settings."""
+    rows = (1 << 24) + 3
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.randn(rows, 2, device="cuda", generator=g)
+    x[::7, 0] = -math.inf
+    x[::21, 1] = -math.inf
+    u = torch.rand(rows, device="cuda", generator=g)
+    k = torch.arange(rows, device="cuda", dtype=torch.int32) % 3  # off, the largest, both
+    ids, logp = bpe.sample(x, u, top_k=k)
+    share = torch.softmax(x.double(), 1)
+    want = torch.where(k == 1, x[:, 1] > x[:, 0], u.double() >= share[:, 0]).int()
+    sure = (share[:, 0] - u.double()).abs() > 2.0 ** -40  # not on the border itself
+    want[::21] = -1
+    sure[::21] = True
+    assert torch.equal(ids[sure], want[sure])
+    assert torch.equal(logp == -math.inf, ids < 0)
+    step = 1 << 22
+    for at in range(0, rows, step):
+        part = slice(at, min(rows, at + step))
+        some = bpe.sample(x[part], u[part], top_k=k[part])
+        assert torch.equal(ids[part], some[0]) and torch.equal(logp[part], some[1])
 
 
 # ---------------------------------------------------------------- decoding
