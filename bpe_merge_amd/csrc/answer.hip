@@ -221,8 +221,15 @@ namespace {
 
 template <typename T, int MT, int NT, int WAVES>
 void launch_rows(const bpek::Product& p, hipStream_t s) {
-    hipLaunchKernelGGL((bpek::k_product_rows<T, MT, NT, WAVES>), dim3((p.n + NT * 16 - 1) / (NT * 16), (p.m + MT * 16 - 1) / (MT * 16)),
-                       dim3(64 * WAVES), 0, s, p);
+    bpek::in_parts(p.m, MT * 16, bpek::GROUPS_IN_Y, [&](size_t at, uint32_t part, uint32_t groups) {
+        bpek::Product here = p;
+        here.a += at * p.as;
+        here.sa += at * p.sas;
+        here.out = static_cast<typename T::raw*>(p.out) + at * p.os;
+        here.m = part;
+        hipLaunchKernelGGL((bpek::k_product_rows<T, MT, NT, WAVES>), dim3((p.n + NT * 16 - 1) / (NT * 16), groups),
+                           dim3(64 * WAVES), 0, s, here);
+    });
 }
 
 template <typename T, bool EXACT, int BN, int BM, int WN, int WM, int STAGES, bpek::Pieces KIND>

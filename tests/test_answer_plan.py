@@ -64,3 +64,17 @@ def test_rows_beyond_a_launch_go_in_parts(plan, threads, group_rows):
             at += part
         assert at == rows
     assert _parts(plan, 0, group_rows, most) == []
+
+
+def test_rows_of_products_beyond_a_launch_go_in_parts(plan):
+    """Workgroups of 16, 32 or 64 rows along y, up to the largest m."""
+    most = plan.groups_in_y()
+    assert most == 65535
+    for group_rows in (16, 32, 64):
+        limit = most * group_rows
+        for rows in (1, limit, limit + 1, 0x7FFF80):
+            parts = _parts(plan, rows, group_rows, most)
+            assert [p[0] for p in parts] == list(range(0, rows, limit)) and sum(p[1] for p in parts) == rows
+            assert all((g - 1) * group_rows < n <= g * group_rows and g <= most for _, n, g in parts)
+    # along x the widest launch has a workgroup of 512 threads for each 16 rows of b
+    assert -(-0x7FFF80 // 16) <= plan.groups_in_x(512)

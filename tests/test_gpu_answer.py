@@ -252,6 +252,40 @@ def test_matmul_scaled_of_rows_in_wider_buffers(bpe, m, n, k, pad):
         _check_product(bpe.matmul_scaled(aw[1:, :k], saw[1:, :blocks], bw[:, :k], sbw[:, :blocks]), a[1:], sa[1:], b, sb)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("far", ["a", "b", "both"])
+def test_matmul_scaled_of_rows_far_apart(bpe, dtype, far):
+    """Rows 2^23 bytes apart and more, which leave a tile's 32-bit offsets."""
+    m, n, k = 70, 20, 300
+    a, sa = _operand(3, m, k, False)
+    b, sb = _operand(4, n, k, True)
+
+    def spread(t, wide):
+        if not wide:
+            return t.cuda()
+        f = torch.full(((t.shape[0] - 1) * ((1 << 23) + 48) + t.shape[1],), 0x7F, dtype=torch.uint8, device="cuda").view(E4M3)
+        v = f.as_strided(t.shape, ((1 << 23) + 48, 1))
+        v.copy_(t)
+        return v
+    out = bpe.matmul_scaled(spread(a, far != "b"), sa.cuda() * 2.0 ** -8, spread(b, far != "a"), sb.cuda() * 2.0 ** -8, out_dtype=dtype)
+    _check_product(out, a, sa * 2.0 ** -8, b, sb * 2.0 ** -8)
+
+
+def test_matmul_scaled_of_more_rows_than_a_launch_takes(bpe):
+    """2^16 workgroups of 64 rows of a, by two rows of b 2^23 bytes apart."""
+    m, n, k = (1 << 22) + 70, 2, 16
+    a, sa = _operand(3, 4096, k, False)
+    b, sb = _operand(4, n, k, True)
+    at = torch.randint(0, 4096, (m,), generator=torch.Generator().manual_seed(5))
+    f = torch.zeros((1 << 23) + k, dtype=torch.uint8, device="cuda").view(E4M3)
+    bw = f.as_strided((n, k), (1 << 23, 1))
+    bw.copy_(b)
+    few = bpe.matmul_scaled(a.cuda(), sa.cuda(), bw, sb.cuda(), out_dtype=torch.float32)
+    _check_product(few, a, sa, b, sb)
+    many = bpe.matmul_scaled(a.view(torch.uint8)[at].view(E4M3).cuda(), sa[at].cuda(), bw, sb.cuda(), out_dtype=torch.float32)
+    assert torch.equal(many, few[at.cuda()])
+
+
 def test_matmul_scaled_rows_do_not_depend_on_one_another(bpe):
     a, sa = (t.cuda() for t in _operand(5, 200, 512, False))
     b, sb = (t.cuda() for t in _operand(6, 300, 512, True))
