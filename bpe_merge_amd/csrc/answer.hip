@@ -219,6 +219,10 @@ bpe_status bpe_quant_weight(const void* w, size_t w_stride, bpe_type type, size_
 
 namespace {
 
+// Results whose inner sums take the exact form for any number of rows.
+template <typename T>
+constexpr bool exact_sums = !std::is_same_v<T, bpek::BF16>;
+
 template <typename T, int MT, int NT, int WAVES>
 void launch_rows(const bpek::Product& p, hipStream_t s) {
     bpek::in_parts(p.m, MT * 16, bpek::GROUPS_IN_Y, [&](size_t at, uint32_t part, uint32_t groups) {
@@ -239,75 +243,35 @@ void launch_tile(const bpek::Product& p, hipStream_t s) {
                        0, s, p, tn, tm);
 }
 
-// Streams over eight parts of K: of the most rows of a that leave a workgroup
-// to nearly every CU (rows of b x rows of a x K, 16, 32 or 64 rows of a to a
-// workgroup: 456 x 128 x 8,192, 11, 17 or 27 us; 2,000 x 64 x 4,096, 11, 10 or
-// 15; 456 x 500 x 4,091, 23, 20 or 18).
+// The kernel that product_kernel names.
 template <typename T>
-void launch_parts(const bpek::Product& p, hipStream_t s) {
-    auto workgroups = [&](uint64_t rows) { return (p.n + 15) / 16 * ((p.m + rows - 1) / rows); };
-    if (p.m > 32 && workgroups(64) >= 200) launch_rows<T, 4, 1, 8>(p, s);
-    else if (p.m > 16 && workgroups(32) >= 200) launch_rows<T, 2, 1, 8>(p, s);
-    else launch_rows<T, 1, 1, 8>(p, s);
+void launch_streams(bpek::ProductKernel kernel, const bpek::Product& p, hipStream_t s) {
+    switch (kernel) {
+        case bpek::PK_PARTS_64: return launch_rows<T, 4, 1, 8>(p, s);
+        case bpek::PK_PARTS_32: return launch_rows<T, 2, 1, 8>(p, s);
+        case bpek::PK_PARTS_16: return launch_rows<T, 1, 1, 8>(p, s);
+        case bpek::PK_STREAM_16: return launch_rows<T, 1, 1, 4>(p, s);
+        case bpek::PK_STREAM_32: return launch_rows<T, 2, 2, 4>(p, s);
+        default: return launch_rows<T, 4, 2, 4>(p, s);
+    }
 }
-
-// Streams for any rows.
-template <typename T>
-void launch_streams(const bpek::Product& p, hipStream_t s) {
-    if (p.n < 512 * 32 && p.blocks >= 16) launch_parts<T>(p, s);
-    else if (p.m <= 16) launch_rows<T, 1, 1, 4>(p, s);
-    else if (p.m <= 32) launch_rows<T, 2, 2, 4>(p, s);
-    else launch_rows<T, 4, 2, 4>(p, s);
-}
-
-// The tile for more than 64 rows, by the time a block of K takes (measured,
-// in us): 256 x 256, one to a CU, 2.1; 256 x 128, one to a CU, 1.15; 128 x
-// 128, 0.85 alone on a CU and 1.55 for two. On 2,048 x 65,536 x 4,096 they
-// take 534, 620 and 775 us; on 1,024 x 8,192 x 8,192, where the widest leave
-// half of the CUs idle, 106, 66 and 78 us. Exact sums (f32 and binary16 results)
-// take 1.6 times as long in each, and have no 256 x 256, whose registers do not
-// hold their fragments (nor anything but full blocks); 128 x 128 alone on a CU
-// then takes 8 waves (128 x 32,256 x 4,096: 41 against 54 us). Pieces that go
-// through registers take the last (700 x 32,256 x 3,909: 215 us, 235 in the
-// second; 142 where rows are whole pieces). Where even of the last there are
-// only a few, streams over parts of K keep more of the chip busy (128 x 456 x
-// 8,192: 66 against 11 us; 1,000 x 456 x 8,191: 86 against 64).
 template <typename T, bpek::Pieces KIND>
-void launch_tiles(const bpek::Product& p, hipStream_t s) {
-    constexpr bool EXACT = !std::is_same_v<T, bpek::BF16>, COPIED = bpek::copied(KIND);
-    constexpr uint64_t CUS = 256;
-    auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
-    auto tiles = [&](uint64_t bn, uint64_t bm) { return up(p.n, bn) * up(p.m, bm); };
-    const uint64_t wide = up(tiles(256, 256), CUS) * 210, mid = up(tiles(256, 128), CUS) * 115;
-    if (tiles(128, 128) <= 40 && p.blocks >= 16) return launch_parts<T>(p, s);
-    const uint64_t narrow = tiles(128, 128) <= CUS ? 85 : up(tiles(128, 128), 2 * CUS) * 155;
-    if constexpr (!EXACT && KIND == bpek::PR_FULL) {
-        if (wide <= mid && wide <= narrow) return launch_tile<T, false, 256, 256, 2, 4, 2, KIND>(p, s);
+void launch_product(bpek::ProductKernel kernel, const bpek::Product& p, hipStream_t s) {
+    constexpr bool EXACT = exact_sums<T>, COPIED = bpek::copied(KIND);
+    switch (kernel) {
+        case bpek::PK_TILE_128_64: return launch_tile<T, true, 128, 64, 2, 2, COPIED ? 3 : 2, KIND>(p, s);
+        case bpek::PK_TILE_256_256:  // (product_kernel names no tile whose condition here does not hold)
+            if constexpr (!EXACT && KIND == bpek::PR_FULL) return launch_tile<T, false, 256, 256, 2, 4, 2, KIND>(p, s);
+            [[fallthrough]];
+        case bpek::PK_TILE_256_128:
+            if constexpr (COPIED) return launch_tile<T, EXACT, 256, 128, 4, 2, 3, KIND>(p, s);
+            [[fallthrough]];
+        case bpek::PK_TILE_128_128_WAVES:
+            if constexpr (EXACT && KIND != bpek::PR_NARROW) return launch_tile<T, EXACT, 128, 128, 2, 4, COPIED ? 3 : 2, KIND>(p, s);
+            [[fallthrough]];
+        case bpek::PK_TILE_128_128: return launch_tile<T, EXACT, 128, 128, 2, 2, 2, KIND>(p, s);
+        default: return launch_streams<T>(kernel, p, s);
     }
-    if constexpr (COPIED) {
-        if (mid <= narrow) return launch_tile<T, EXACT, 256, 128, 4, 2, 3, KIND>(p, s);
-    }
-    if constexpr (EXACT && KIND != bpek::PR_NARROW) {
-        if (tiles(128, 128) <= CUS) return launch_tile<T, EXACT, 128, 128, 2, 4, COPIED ? 3 : 2, KIND>(p, s);
-    }
-    launch_tile<T, EXACT, 128, 128, 2, 2, 2, KIND>(p, s);
-}
-
-// Up to 64 rows. Streaming b costs a read of a's rows beside every read of
-// b's, so that 4 rows already take longer than through LDS (64,256 x 4,096,
-// 16 rows: 87 against 55 us; 4 rows: 62; 1 row: 50 us); but a tile is 128 rows
-// of b, and where there are few of them streams over parts of K keep more busy
-// (61 rows x 4,352: 23 against 27 us for 4,256 rows of b, 45 against 30 us for
-// 16,256). Rows that are not whole pieces go through LDS one block ahead only,
-// which pays from more 16 x 16 tiles on (streams against LDS: 60 x 8,256 x
-// 1,001, 10 against 13 us; 5 x 32,256 x 4,001, 47 against 57; 61 x 16,256 x
-// 4,353, 75 against 50; 16 x 64,256 x 4,095, 133 against 71).
-template <typename T, bpek::Pieces KIND>
-void launch_few(const bpek::Product& p, hipStream_t s) {
-    constexpr bool COPIED = bpek::copied(KIND);
-    const bool tile = COPIED ? p.m > 3 && p.n >= 128 * 48 : p.m > 8 && (p.m + 15) / 16 * size_t(p.n) >= 48000;
-    if (tile) launch_tile<T, true, 128, 64, 2, 2, COPIED ? 3 : 2, KIND>(p, s);
-    else launch_streams<T>(p, s);
 }
 
 }  // namespace
@@ -362,20 +326,15 @@ bpe_status bpe_matmul_scaled(const uint8_t* a, size_t a_stride, const float* a_s
     // tiles need 256 rows within 32-bit offsets, copies whole aligned pieces
     // of 16 bytes
     const bool tiled = (m == 1 || a_stride < (1u << 23)) && (n == 1 || b_stride < (1u << 23));
-    const bool pieces = k % 16 == 0 && aligned(a, 16) && aligned(b, 16) && (m == 1 || a_stride % 16 == 0) &&
-                        (n == 1 || b_stride % 16 == 0);
+    const bool aligned_rows = aligned(a, 16) && aligned(b, 16) && (m == 1 || a_stride % 16 == 0) && (n == 1 || b_stride % 16 == 0);
+    const bpek::Pieces kind = bpek::pieces_of(k, aligned_rows);
     with_type(out_type, [&](auto tag) {
         using T = decltype(tag);
-        auto launch = [&](auto kind) {
-            constexpr bpek::Pieces KIND = decltype(kind)::value;
-            if (m <= 64) launch_few<T, KIND>(p, s);
-            else launch_tiles<T, KIND>(p, s);
-        };
-        if (!tiled) launch_streams<T>(p, s);
-        else if (k < 128) launch(std::integral_constant<bpek::Pieces, bpek::PR_NARROW>{});
-        else if (!pieces) launch(std::integral_constant<bpek::Pieces, bpek::PR_ODD>{});
-        else if (k % 128 == 0) launch(std::integral_constant<bpek::Pieces, bpek::PR_FULL>{});
-        else launch(std::integral_constant<bpek::Pieces, bpek::PR_SHORT>{});
+        const bpek::ProductKernel kernel = bpek::product_kernel(m, n, blocks, kind, exact_sums<T>, tiled);
+        if (kind == bpek::PR_NARROW) launch_product<T, bpek::PR_NARROW>(kernel, p, s);
+        else if (kind == bpek::PR_ODD) launch_product<T, bpek::PR_ODD>(kernel, p, s);
+        else if (kind == bpek::PR_FULL) launch_product<T, bpek::PR_FULL>(kernel, p, s);
+        else launch_product<T, bpek::PR_SHORT>(kernel, p, s);
     });
     HIP_TRY(hipGetLastError());
     return BPE_OK;

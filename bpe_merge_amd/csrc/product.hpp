@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "lanes.hpp"
+#include "plan.hpp"
 
 namespace bpek {
 
@@ -267,14 +268,6 @@ __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)p; }
-
-enum Pieces {
-    PR_FULL,    // copied: rows of whole blocks, aligned to 16 bytes
-    PR_SHORT,   // copied: rows of whole pieces (128 bytes at least), aligned to 16 bytes
-    PR_ODD,     // through registers: rows of 128 bytes at least
-    PR_NARROW   // through registers: rows of fewer, one block
-};
-constexpr bool copied(Pieces kind) { return kind == PR_FULL || kind == PR_SHORT; }
 
 template <typename T, bool EXACT, int BN, int BM, int WN, int WM, int STAGES, Pieces KIND>
 __global__ __launch_bounds__(64 * WN * WM) void k_product_tile(Product p, uint32_t tiles_n, uint32_t tiles_m) {

@@ -73,6 +73,27 @@ def product_dropped(a, sa, b, sb):
     return out
 
 
+# Products that between them take every kernel there is (see
+# test_answer_plan.py, which asks the library's own rule), each with what rows
+# of a cover: (m, n, k).
+PRODUCTS = [
+    # streams over parts of K: 16, 32 and 64 rows of a
+    (2, 1700, 2048), (30, 3300, 2049), (61, 4256, 2064), (130, 456, 2064), (600, 456, 2049),
+    # streams: up to 16, 32 and 64 rows
+    (1, 20000, 400), (9, 700, 100), (30, 1000, 272), (60, 700, 513),
+    # 128 x 64 tiles: whole, short and odd rows, and rows of less than a block
+    (5, 6200, 256), (64, 6200, 400), (33, 16100, 401), (64, 12500, 100),
+    # 256 x 256, with few and with many blocks of K
+    (520, 16640, 384), (500, 32700, 2048),
+    # 256 x 128: whole and short rows
+    (600, 8256, 1024), (515, 8000, 528), (600, 16500, 272),
+    # 128 x 128 by four waves: whole, short and odd rows, and rows of less than a block
+    (789, 9244, 128), (789, 9244, 144), (200, 1000, 512), (200, 1000, 528), (515, 9000, 529), (300, 700, 100),
+    # by eight waves (exact sums): whole, short and odd rows
+    (128, 12500, 256), (128, 12500, 272), (128, 12500, 257),
+]
+
+
 def draw(row, u, temperature, top_k, top_p, min_p):
     """(id, log of its share) for one row of logits, by the definition: NaN
     never kept, +inf the largest finite f32."""

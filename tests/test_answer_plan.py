@@ -6,6 +6,8 @@ import subprocess
 
 import pytest
 
+import answers
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 SOURCE = """
@@ -22,6 +24,13 @@ int parts(uint64_t rows, uint64_t group_rows, uint64_t most_groups, uint64_t *ou
     });
     return n;
 }
+int kernels() { return bpek::PK_COUNT; }
+int first_tile() { return bpek::PK_TILE_128_64; }
+// the kernel of a product and the kind of its pieces
+int kernel(uint64_t m, uint64_t n, uint64_t k, int aligned_rows, int exact, int tiled, int *kind) {
+    *kind = bpek::pieces_of(k, aligned_rows);
+    return bpek::product_kernel(m, n, (k + 127) / 128, bpek::Pieces(*kind), exact, tiled);
+}
 }
 """
 
@@ -36,6 +45,7 @@ def plan(tmp_path_factory):
     lib = ctypes.CDLL(str(lib))
     u64 = ctypes.c_uint64
     lib.groups_in_x.argtypes, lib.groups_in_x.restype, lib.groups_in_y.restype = [u64], u64, u64
+    lib.kernel.argtypes = [u64, u64, u64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     lib.parts.argtypes = [u64, u64, u64, ctypes.POINTER(u64), ctypes.c_int]
     return lib
 
@@ -78,3 +88,38 @@ def test_rows_of_products_beyond_a_launch_go_in_parts(plan):
             assert all((g - 1) * group_rows < n <= g * group_rows and g <= most for _, n, g in parts)
     # along x the widest launch has a workgroup of 512 threads for each 16 rows of b
     assert -(-0x7FFF80 // 16) <= plan.groups_in_x(512)
+
+
+def _kernel(plan, m, n, k, aligned_rows, exact, tiled=True):
+    """What a product runs: (kernel, kind of its pieces where it is a tile)."""
+    kind = ctypes.c_int()
+    kernel = plan.kernel(m, n, k, aligned_rows, exact, tiled, ctypes.byref(kind))
+    assert 0 <= kernel < plan.kernels()
+    return kernel, kind.value if kernel >= plan.first_tile() else None
+
+
+@pytest.mark.parametrize("exact", [False, True])
+def test_the_products_tested_take_every_kernel(plan, exact):
+    """Every kernel and kind of pieces that a sweep over sizes meets is taken
+    by one of answers.PRODUCTS, whose rows the library is given aligned."""
+    sizes = sorted({int(f * 2 ** e) + d for e in range(15) for f in (1, 1.25, 1.6) for d in (-1, 0, 1)} - {-1, 0})
+    met = {}
+    for m in sizes[::2]:
+        for n in sizes[::2] + [33000, 65536]:
+            for k in (64, 128, 130, 144, 1024, 1025, 1040, 2048, 2049, 2064, 8192):
+                for aligned_rows in (0, 1):
+                    met.setdefault(_kernel(plan, m, n, k, aligned_rows, exact), (m, n, k))
+    tested = {_kernel(plan, m, n, k, 1, exact) for m, n, k in answers.PRODUCTS}
+    assert {what: size for what, size in met.items() if what not in tested} == {}
+    assert tested <= set(met)
+    deep = [p for p in answers.PRODUCTS if _kernel(plan, *p, 1, False) == _kernel(plan, 520, 16640, 384, 1, False)]
+    assert max(k for _, _, k in deep) >= 2048  # the widest tile over many blocks of K too
+    names = {kernel for kernel, _ in met}
+    # all kernels there are, but for those of the other form of sums: the widest
+    # tile, and the tile of eight waves
+    assert len(names) == plan.kernels() - 1
+
+
+def test_rows_far_apart_take_streams(plan):
+    for m, n, k in answers.PRODUCTS:
+        assert _kernel(plan, m, n, k, 1, True, tiled=False)[0] < plan.first_tile()

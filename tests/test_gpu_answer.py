@@ -253,6 +253,29 @@ def test_matmul_scaled_of_rows_in_wider_buffers(bpe, m, n, k, pad):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m, n, k", answers.PRODUCTS)
+def test_matmul_scaled_by_every_kernel(bpe, dtype, m, n, k):
+    """Looked at as in the test of every tile, in every type."""
+    a, sa = _operand(m, m, k, False)
+    b, sb = _operand(n, n, k, True)
+    if dtype == torch.float16:  # kept inside its range
+        sa, sb = sa * 2.0 ** -14, sb * 2.0 ** -8
+    last = (n - 1) // 128
+    take = sorted({0, 1, last // 2, last - 1, last})
+    columns = [c for block in take for c in range(block * 128, min(n, block * 128 + 128))]
+    rows = sorted({0, m // 2, m - 1} | set(range(0, m, max(1, m // 40))))
+    out = bpe.matmul_scaled(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), out_dtype=dtype)
+    want, size = answers.product(a[rows], sa[rows], b[columns], sb[take])
+    got = out[rows][:, columns].double().cpu().numpy()
+    tol = answers.product_tolerance(size, sa.shape[1]) + answers.half_step(dtype) * np.abs(want)
+    if dtype == torch.bfloat16 and m > 64:
+        tol += answers.product_dropped(a[rows], sa[rows], b[columns], sb[take])
+    tol = tol * (1 + 2.0 ** -8) + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    assert dtype != torch.float16 or np.abs(want).max() < 65504
+    assert np.all(np.abs(got - want) <= tol)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("far", ["a", "b", "both"])
 def test_matmul_scaled_of_rows_far_apart(bpe, dtype, far):
     """Rows 2^23 bytes apart and more, which leave a tile's 32-bit offsets."""
