@@ -11,6 +11,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -722,8 +723,12 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         if isinstance(value, torch.Tensor):
             if _cuda(value, name).numel() != rows:
                 raise ValueError("%s must be a number or have one value for each row" % name)
+            if dtype == torch.int32 and value.dtype != dtype:  # what passes 32 bits is all of a row, as SAMPLE_MAX_VOCAB is
+                value = (value.double() if value.is_floating_point() else value.long()).clamp(0, SAMPLE_MAX_VOCAB)
             held.append(value.to(dtype).contiguous())
             setattr(how, name + "s", held[-1].data_ptr())
+        elif dtype == torch.int32:  # a ctypes field would keep the low 32 bits of it
+            setattr(how, name, max(-1, min(operator.index(value), 0x7FFFFFFF)))
         else:
             setattr(how, name, value)
     u = u.contiguous()

@@ -132,6 +132,55 @@ def test_the_binding_refuses_host_tensors_and_wrong_types(bpe):
         bpe.sample(x, torch.zeros(4))
 
 
+class Recorder:
+    """In the library's place: keeps what bpe_sample is called with."""
+
+    def bpe_sample(self, logits, stride, kind, rows, vocab, u, how, ids, logp, stream):
+        h = how._obj
+        self.top_k = h.top_k
+        self.top_ks = list((ctypes.c_int32 * rows).from_address(h.top_ks)) if h.top_ks else None
+        return 0
+
+
+@pytest.fixture
+def recorder(bpe, monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(bpe, "_lib", r)
+    monkeypatch.setattr(bpe, "_cuda", lambda t, name, dtype=None: t)
+    monkeypatch.setattr(bpe, "_stream_handle", lambda device: None)
+    return r
+
+
+def test_a_top_k_past_32_bits_is_not_another_one(bpe, recorder):
+    x, u = torch.zeros(2, 40), torch.zeros(2)
+    for given in (0, 1, 7, 0x7FFFFFFF, 1 << 20):
+        bpe.sample(x, u, top_k=given)
+        assert recorder.top_k == given
+    for given in (1 << 31, (1 << 32) + 1, 1 << 32, 1 << 80):  # all of a row
+        bpe.sample(x, u, top_k=given)
+        assert recorder.top_k >= bpe.SAMPLE_MAX_VOCAB
+    for given in (-1, -(1 << 31) - 1, -(1 << 32) + 5):  # for the library to refuse
+        bpe.sample(x, u, top_k=given)
+        assert recorder.top_k < 0
+    with pytest.raises(TypeError):
+        bpe.sample(x, u, top_k=5.0)
+
+
+def test_row_top_ks_past_32_bits_are_not_other_ones(bpe, recorder):
+    x, u = torch.zeros(5, 40), torch.zeros(5)
+    bpe.sample(x, u, top_k=torch.tensor([0, 1, -3, 1 << 30, 7], dtype=torch.int32))
+    assert recorder.top_ks == [0, 1, -3, 1 << 30, 7]
+    bpe.sample(x, u, top_k=torch.tensor([3, (1 << 32) + 1, 1 << 31, -(1 << 32) + 5, 0]))
+    k = recorder.top_ks
+    assert k[0] == 3 and k[1] >= bpe.SAMPLE_MAX_VOCAB and k[2] >= bpe.SAMPLE_MAX_VOCAB and k[3] <= 0 and k[4] == 0
+    for dtype in (torch.uint8, torch.int16):
+        bpe.sample(x, u, top_k=torch.tensor([3, 100, 0, 1, 7], dtype=dtype))
+        assert recorder.top_ks == [3, 100, 0, 1, 7]
+    bpe.sample(x, u, top_k=torch.tensor([3.0, 1e30, 0.0, -1e30, 7.0]))
+    k = recorder.top_ks
+    assert k[0] == 3 and k[1] >= bpe.SAMPLE_MAX_VOCAB and k[2] == 0 and k[3] <= 0 and k[4] == 7
+
+
 # the 64-bit forms themselves
 
 def test_the_plain_draw_by_hand():
