@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import operator
 import os
+import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbpe.so")
@@ -742,11 +743,13 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
 class Decoder:
     """bpe_decoder_build ... bpe_decoder_free: ids back to text with the
     vocabulary of a merge list ([k, 2] or [k, 3]; merge i is id 256 + i), on
-    the current CUDA device."""
+    the current CUDA device. Calls on one decoder from several threads take
+    turns; threads that should not wait have decoders of their own."""
 
     def __init__(self, merges):
         torch = _torch()
         self._h = _vp(None)
+        self._turn = threading.Lock()
         dev = torch.device("cuda", torch.cuda.current_device())
         m = _merge_list(merges, dev)
         self.device = dev
@@ -778,12 +781,13 @@ class Decoder:
             # hold says its length, and is written on a second call
             out = torch.empty(min(8 * n + 64, n * self._longest), dtype=torch.uint8, device=tokens.device)
         n_bytes = _sz(0)
-        while True:
-            st = _lib.bpe_decoder_decode(self._h, tokens.data_ptr(), n, _stream_handle(tokens.device), out.data_ptr() or None,
-                                         out.numel(), places.data_ptr() if offsets else None, ctypes.byref(n_bytes))
-            if given or st != EINVAL or n_bytes.value <= out.numel():
-                break
-            out = torch.empty(n_bytes.value, dtype=torch.uint8, device=tokens.device)
+        with self._turn:  # the interpreter's lock is not held during the call
+            while True:
+                st = _lib.bpe_decoder_decode(self._h, tokens.data_ptr(), n, _stream_handle(tokens.device), out.data_ptr() or None,
+                                             out.numel(), places.data_ptr() if offsets else None, ctypes.byref(n_bytes))
+                if given or st != EINVAL or n_bytes.value <= out.numel():
+                    break
+                out = torch.empty(n_bytes.value, dtype=torch.uint8, device=tokens.device)
         _check(st, "bpe_decoder_decode")
         if n_bytes.value > out.numel():  # an empty out is passed as none
             raise ValueError("out has no room for the text's %d bytes" % n_bytes.value)
@@ -791,9 +795,10 @@ class Decoder:
         return (text, places) if offsets else text
 
     def free(self) -> None:
-        if self._h:
-            _lib.bpe_decoder_free(self._h)
-            self._h = _vp(None)
+        with self._turn:
+            if self._h:
+                _lib.bpe_decoder_free(self._h)
+                self._h = _vp(None)
 
     def __enter__(self):
         return self

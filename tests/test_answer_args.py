@@ -1,6 +1,8 @@
 """What the operators between a hidden state and text refuse, through the C ABI
 and the binding, without a device: every check here comes before any launch."""
 import ctypes
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -179,6 +181,75 @@ def test_row_top_ks_past_32_bits_are_not_other_ones(bpe, recorder):
     bpe.sample(x, u, top_k=torch.tensor([3.0, 1e30, 0.0, -1e30, 7.0]))
     k = recorder.top_ks
     assert k[0] == 3 and k[1] >= bpe.SAMPLE_MAX_VOCAB and k[2] == 0 and k[3] <= 0 and k[4] == 7
+
+
+def test_threads_that_share_a_decoder_take_turns(bpe, monkeypatch):
+    """Calls on one decoder must not overlap, nor one with its end; the
+    interpreter's lock is not held during a call."""
+    class Busy:
+        inside = most = calls = freed = 0
+
+        def enter(self):
+            self.inside += 1
+            self.most = max(self.most, self.inside)
+            time.sleep(0.002)
+            self.inside -= 1
+
+        def bpe_decoder_decode(self, handle, tokens, n, stream, out, room, places, n_bytes):
+            self.calls += 1
+            self.enter()
+            n_bytes._obj.value = 0
+            return 0 if handle.value and not self.freed else bpe.EINVAL
+
+        def bpe_last_error(self):
+            return b"freed"
+
+        bpe_strerror = lambda self, status: b"invalid"  # noqa: E731
+
+        def bpe_decoder_free(self, handle):
+            self.enter()
+            self.freed += 1
+
+        def bpe_decoder_info(self, handle, vocab, longest):
+            longest._obj.value = 1
+            return 0
+
+        def bpe_decoder_build(self, merges, n, handle):
+            handle._obj.value = 1
+            return 0
+
+    busy = Busy()
+    monkeypatch.setattr(bpe, "_lib", busy)
+    monkeypatch.setattr(bpe, "_cuda", lambda t, name, dtype=None: t)
+    monkeypatch.setattr(bpe, "_stream_handle", lambda device: None)
+    monkeypatch.setattr(bpe, "_merge_list", lambda merges, device: torch.zeros(0, 3, dtype=torch.int32))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    d = bpe.Decoder([])
+    tokens, failed = torch.zeros(3, dtype=torch.int32), []
+
+    def work(times):
+        try:
+            for _ in range(times):
+                d.decode(tokens)
+                time.sleep(0.0005)
+        except Exception as e:
+            failed.append(e)
+    try:
+        threads = [threading.Thread(target=work, args=(10,)) for _ in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failed and busy.calls == 40 and busy.most == 1
+        late = threading.Thread(target=work, args=(5000,))  # meets free(): the library's error for no decoder
+        late.start()
+        time.sleep(0.003)
+        d.free()
+        late.join()
+        assert busy.freed == 1 and busy.most == 1
+        assert len(failed) == 1 and isinstance(failed[0], bpe.BpeError)
+    finally:
+        d._h = ctypes.c_void_p(None)  # not the library's to release
 
 
 # the 64-bit forms themselves

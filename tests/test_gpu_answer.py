@@ -2,6 +2,7 @@
 against plain 64-bit forms (tests/answers.py)."""
 import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -609,6 +610,30 @@ def test_decode_of_the_whole_id_space(bpe):
         # more text than was made room for at first
         many = torch.full((5000,), int(np.argmax([len(t) for t in text])), dtype=torch.int32, device="cuda")
         assert d.decode(many).cpu().numpy().tobytes() == max(text, key=len) * 5000
+
+
+def test_decode_from_several_threads(bpe, vocabulary):
+    """Texts of different lengths through one decoder, by one pass and by two."""
+    merges, text = vocabulary
+    failed = []
+    with bpe.Decoder(merges) as d:
+        def work(seed):
+            try:
+                with torch.cuda.stream(torch.cuda.Stream()):
+                    r = np.random.RandomState(seed)
+                    for n in (5, 3000, 60, 20000, 1, 2500) * 4:
+                        ids = r.randint(0, len(text), n).astype(np.int32)
+                        got, places = d.decode(torch.from_numpy(ids).cuda(), offsets=True)
+                        assert got.cpu().numpy().tobytes() == b"".join(text[i] for i in ids.tolist())
+                        assert int(places[-1]) == got.numel()
+            except Exception as e:
+                failed.append(e)
+        threads = [threading.Thread(target=work, args=(seed,)) for seed in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    assert not failed, failed
 
 
 def test_decode_gives_encoded_text_back(bpe):
