@@ -395,6 +395,7 @@ void bpe_trie_free(bpe_trie *t);
    output is in 8 bits (bpe_norm_quant), the product of its rows with the
    vocabulary's output matrix (bpe_matmul_scaled), an id drawn from each row
    of logits (bpe_sample), and the ids' bytes (bpe_decoder_decode).
+   They serve: none has a gradient.
    bpe_norm_quant, bpe_quant_weight, bpe_matmul_scaled and bpe_sample only
    enqueue work on stream (a hipStream_t; NULL: the null stream), allocate
    nothing and may be captured into a graph. Their arrays are device memory

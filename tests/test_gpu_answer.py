@@ -86,6 +86,16 @@ def test_norm_quant_in_place_strided_and_more_dimensions(bpe, dtype):
     assert q.shape == (d,) and s.shape == (6,)
 
 
+def test_no_gradients_pass_through(bpe):
+    x = _randn(1, 3, 256).cuda().requires_grad_()
+    w = torch.ones(256).cuda().requires_grad_()
+    q, s, h = bpe.norm_quant(x, w, residual=x)
+    b, sb = bpe.quant_weight(x)
+    logits = bpe.matmul_scaled(q, s, b, sb, out_dtype=torch.float32)
+    ids, logp = bpe.sample(logits.requires_grad_(), torch.rand(3).cuda())
+    assert not any(t.requires_grad for t in (q, s, h, b, sb, ids, logp))
+
+
 def test_norm_quant_of_zeros_extremes_and_no_numbers(bpe):
     d = 300
     w = torch.ones(d).cuda()
