@@ -166,10 +166,10 @@ bpe_status bpe_norm_quant(const void* x, size_t x_stride, const void* residual, 
                                    scales + at * ((d + 127) / 128));
             });
         };
-        // The fewest lanes that hold a row in at most 32 columns each: a wave
-        // up to 1,024 columns (4 rows in a workgroup, no barrier), 4 waves up
-        // to 8,192 (more lanes with fewer columns would wait for each other's
-        // sums more often), 16 waves beyond.
+        // A wave up to 1,024 columns (16 of them a lane; 4 rows in a
+        // workgroup, no barrier), 4 waves up to 8,192 (32 a lane; more lanes
+        // with fewer columns would wait for each other's sums more often),
+        // 16 waves beyond (64 a lane).
         if (d <= 512) launch(bpek::k_norm_quant<T, 1, 1>, 4, 256);
         else if (d <= 1024) launch(bpek::k_norm_quant<T, 1, 2>, 4, 256);
         else if (d <= 2048) launch(bpek::k_norm_quant<T, 4, 1>, 1, 256);

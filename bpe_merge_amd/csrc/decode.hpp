@@ -18,7 +18,7 @@
 //
 // Measured: 8,000,003 ids of a vocabulary of 32,256 (58 MB of text): 15 us for
 // the sums, 43 us for the text, where every id's entry is a gather from the L2
-// (a line for 16 bytes of it); 64 ids: 6 us, 11 us until the host, which polls a
+// (a line for 16 bytes of it); 64 ids: 7 us, 11 us until the host, which polls a
 // word for the end, has their length (16 us where it waits for the stream).
 #pragma once
 

@@ -69,14 +69,8 @@ __device__ __forceinline__ V wave_all(V v, V ident, Op op) {
     return read_lane(wave_inclusive(v, ident, op), 63);
 }
 
-__device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
-    return wave_all(v, 0u, [](uint32_t a, uint32_t b) { return a + b; });
-}
 __device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
     return wave_all(v, uint64_t(0), [](uint64_t a, uint64_t b) { return a + b; });
-}
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-    return wave_all(v, uint64_t(0), [](uint64_t a, uint64_t b) { return a > b ? a : b; });
 }
 __device__ __forceinline__ double wave_sum(double v) {
     v += lane_move<LN_SWAP1>(v);
