@@ -634,6 +634,18 @@ bpe_status bpe_decoder_decode(bpe_decoder* d, const uint32_t* tokens, size_t n, 
     if (n && (st = place_of("tokens", tokens, d->device, &tokens_host)) != BPE_OK) return st;
     if (bytes && (st = place_of("bytes", bytes, d->device, &bytes_host)) != BPE_OK) return st;
     if (offsets && (st = place_of("offsets", offsets, d->device, &offsets_host)) != BPE_OK) return st;
+    // The second pass reads the tokens while it writes, and writes where the
+    // first pass's lengths say: on one device none may share memory. (What
+    // lies in host memory is copied on the way.)
+    const void* given[3] = {tokens, bytes, offsets};
+    const uint64_t size[3] = {n * sizeof(uint32_t), bytes_cap, (n + 1) * sizeof(int64_t)};
+    const bool there[3] = {n && !tokens_host, bytes && !bytes_host, offsets && !offsets_host};
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < i; ++j)
+            if (there[i] && there[j] && bpek::share_bytes(given[i], size[i], given[j], size[j])) {
+                set_err("tokens, bytes and offsets must not share memory");
+                return BPE_EINVAL;
+            }
     const uint32_t* src = tokens;
     if (tokens_host) {
         if ((st = room(&d->tok_buf, &d->tok_cap, n)) != BPE_OK) return st;

@@ -1,6 +1,6 @@
 // How calls of the operators between a hidden state and text are cut into
-// launches: host arithmetic on sizes alone, so that it can be checked without
-// a device.
+// launches, and which arrays may not share memory: host arithmetic on sizes
+// alone, so that it can be checked without a device.
 #pragma once
 
 #include <stdint.h>
@@ -21,6 +21,12 @@ void in_parts(uint64_t rows, uint64_t group_rows, uint64_t most_groups, F f) {
         const uint64_t part = rows - at < most ? rows - at : most;
         f(at, uint32_t(part), uint32_t((part + group_rows - 1) / group_rows));
     }
+}
+
+// Whether two arrays of so many bytes share any.
+inline bool share_bytes(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+    const uint64_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return a_bytes && b_bytes && p < q + b_bytes && q < p + a_bytes;
 }
 
 // ---------------------------------------------------------------- product

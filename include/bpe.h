@@ -512,17 +512,18 @@ bpe_status bpe_decoder_info(const bpe_decoder *d, uint32_t *vocab, uint32_t *max
    or without the word-start bit, as training, encoding, inference and
    bpe_sample give them; 0xFFFFFFFF (bpe_sample's -1) is no token and has no
    bytes. stream: a hipStream_t, or NULL for the decoder's own. Each array is
-   host memory or device memory of the decoder's device.
+   host memory or device memory of the decoder's device; arrays on the device
+   must not share any.
      bytes    out, or NULL for the length only; bytes_cap its room
      offsets  out (n + 1 entries), or NULL: where each token's bytes begin,
               and the whole length
      n_bytes  out (host): the text's length
    Waits for its work to end. The decoder keeps what a call needs between its two
    passes and device copies of host arrays, so calls on one decoder must not
-   overlap. Errors: BPE_EINVAL (NULL arguments, n > BPE_MAX_BYTES, a
-   token that names no id: *n_bytes is 0; bytes_cap below the text's length:
-   *n_bytes is that length; bytes is not written in either case), BPE_ENOMEM,
-   BPE_EHIP. */
+   overlap. Errors: BPE_EINVAL (NULL arguments, n > BPE_MAX_BYTES, device
+   arrays that share memory, a token that names no id: *n_bytes is 0; bytes_cap
+   below the text's length: *n_bytes is that length; bytes is not written in
+   any of these cases), BPE_ENOMEM, BPE_EHIP. */
 bpe_status bpe_decoder_decode(bpe_decoder *d, const uint32_t *tokens, size_t n, void *stream, uint8_t *bytes,
                               size_t bytes_cap, int64_t *offsets, size_t *n_bytes);
 

@@ -24,6 +24,9 @@ int parts(uint64_t rows, uint64_t group_rows, uint64_t most_groups, uint64_t *ou
     });
     return n;
 }
+int share_bytes(uint64_t a, uint64_t a_bytes, uint64_t b, uint64_t b_bytes) {
+    return bpek::share_bytes((const void*)a, a_bytes, (const void*)b, b_bytes);
+}
 int kernels() { return bpek::PK_COUNT; }
 int first_tile() { return bpek::PK_TILE_128_64; }
 // the kernel of a product and the kind of its pieces
@@ -46,6 +49,7 @@ def plan(tmp_path_factory):
     u64 = ctypes.c_uint64
     lib.groups_in_x.argtypes, lib.groups_in_x.restype, lib.groups_in_y.restype = [u64], u64, u64
     lib.kernel.argtypes = [u64, u64, u64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
+    lib.share_bytes.argtypes = [u64] * 4
     lib.parts.argtypes = [u64, u64, u64, ctypes.POINTER(u64), ctypes.c_int]
     return lib
 
@@ -88,6 +92,12 @@ def test_rows_of_products_beyond_a_launch_go_in_parts(plan):
             assert all((g - 1) * group_rows < n <= g * group_rows and g <= most for _, n, g in parts)
     # along x the widest launch has a workgroup of 512 threads for each 16 rows of b
     assert -(-0x7FFF80 // 16) <= plan.groups_in_x(512)
+
+
+def test_arrays_that_share_memory(plan):
+    for a, n, b, m, want in [(0, 10, 10, 5, 0), (10, 5, 0, 10, 0), (0, 10, 9, 5, 1), (9, 5, 0, 10, 1), (0, 100, 40, 1, 1),
+                             (40, 1, 0, 100, 1), (7, 3, 7, 3, 1), (7, 0, 7, 3, 0), (7, 3, 7, 0, 0), (5, 0, 0, 100, 0)]:
+        assert plan.share_bytes(0x1000 + a, n, 0x1000 + b, m) == want
 
 
 def _kernel(plan, m, n, k, aligned_rows, exact, tiled=True):

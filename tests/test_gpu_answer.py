@@ -609,6 +609,24 @@ def test_decode_refuses_bad_tokens_and_small_buffers(bpe, vocabulary):
             d.decode(torch.zeros(4, dtype=torch.int64, device="cuda"))
 
 
+def test_decode_refuses_arrays_that_share_memory(bpe, vocabulary):
+    merges, _ = vocabulary
+    with bpe.Decoder(merges) as d:
+        for n in (10, 5000):
+            held = torch.zeros(3 * n + 8, dtype=torch.int32, device="cuda")
+            ids, memory = held[:n], held.view(torch.uint8)
+            for out in (memory, memory[:n], memory[4 * n - 1:], ids[n // 2:].view(torch.uint8)):
+                with pytest.raises(bpe.BpeError, match="share"):
+                    d.decode(ids, out=out)
+            n_bytes = ctypes.c_size_t(0)
+            places = held.data_ptr() + 8 * (n // 4)
+            for args in ((None, 0, places), (held.data_ptr() + 8 * n, n, held.data_ptr() + 4 * n)):
+                assert bpe._lib.bpe_decoder_decode(d._h, ids.data_ptr(), n, None, *args, ctypes.byref(n_bytes)) == bpe.EINVAL
+            assert not bool(held.any())
+            # side by side is fine
+            assert d.decode(ids, out=memory[4 * n:]).tolist() == [0] * n
+
+
 def test_decode_of_the_whole_id_space(bpe):
     merges = answers.merge_list(65280, 9, longest=15)
     text = answers.strings(merges)
