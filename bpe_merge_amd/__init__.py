@@ -599,7 +599,7 @@ def norm_quant(x, weight, residual=None, eps: float = 1e-5, sum_out=None):
     weight [d], all of one type. Returns (q, scales, h): float8_e4m3fn
     [..., d], float32 [..., ceil(d / 128)], and h in x's type (written to
     sum_out if given: a tensor of x's shape with adjacent columns, which may
-    be residual or x itself). For inference: like the other operators of this
+    be residual or x itself, but not overlap them otherwise). For inference: like the other operators of this
     kind it passes no gradients on, and h comes back detached whatever x
     requires."""
     torch = _torch()

@@ -143,6 +143,12 @@ bpe_status bpe_norm_quant(const void* x, size_t x_stride, const void* residual, 
         return BPE_EINVAL;
     }
     const size_t es = size_of(type);
+    if ((sum && sum != x && bpek::share_rows(sum, sum_stride * es, x, x_stride * es, rows, d * es)) ||
+        (sum && residual && sum != residual &&
+         bpek::share_rows(sum, sum_stride * es, residual, residual_stride * es, rows, d * es))) {
+        set_err("a sum may be x or residual itself, or must share no memory with them");
+        return BPE_EINVAL;
+    }
     if (!aligned(x, es) || !aligned(residual, es) || !aligned(weight, es) || !aligned(sum, es) || !aligned(scales, 4)) {
         set_err("an array is not aligned to its element type");
         return BPE_EINVAL;

@@ -29,6 +29,16 @@ inline bool share_bytes(const void* a, uint64_t a_bytes, const void* b, uint64_t
     return a_bytes && b_bytes && p < q + b_bytes && q < p + a_bytes;
 }
 
+// The same for two arrays of rows of so many bytes, strides (in bytes) apart.
+// Rows of one stride may lie between each other; of two they may not.
+inline bool share_rows(const void* a, uint64_t a_stride, const void* b, uint64_t b_stride, uint64_t rows, uint64_t width) {
+    if (!rows || !share_bytes(a, (rows - 1) * a_stride + width, b, (rows - 1) * b_stride + width)) return false;
+    if (rows == 1 || a_stride != b_stride) return true;
+    const uint64_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    const uint64_t off = (p < q ? q - p : p - q) % a_stride;
+    return off < width || off + width > a_stride;
+}
+
 // ---------------------------------------------------------------- product
 
 enum Pieces {

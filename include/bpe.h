@@ -417,7 +417,8 @@ typedef enum {
    shorter. A block with a value that is no number (NaN in x, residual or
    weight, an infinite h, zeros alone with an eps of 0) has no number as its
    scale or in q.
-     sum     out, or NULL: h. May be x or residual itself (same stride)
+     sum     out, or NULL: h. May be x or residual itself (same stride), and
+             share no memory with them otherwise
      q       out, rows x d
      scales  out, rows x ceil(d / 128), without gaps
    Errors: BPE_EINVAL (d of 0 or above BPE_NORM_MAX_WIDTH, a stride below d,

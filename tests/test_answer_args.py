@@ -44,6 +44,22 @@ def test_norm_quant_of_no_rows_needs_no_device(bpe):
     assert _norm(bpe, rows=0, x=None, w=None, q=None, s=None) == bpe.OK
 
 
+@pytest.mark.parametrize("change", [
+    dict(sum=P + 4, ss=256), dict(sum=P + 1024, ss=256), dict(sum=P + 1020, ss=300), dict(x=P + 8192, r=P, rs=256, sum=P + 2044, ss=256),
+    dict(sum=P, ss=256, r=P + 512, rs=256)])
+def test_norm_quant_refuses_a_sum_over_part_of_its_inputs(bpe, change):
+    assert _norm(bpe, **change) == bpe.EINVAL
+    assert "share no memory" in bpe._lib.bpe_last_error().decode()
+
+
+@pytest.mark.parametrize("change", [
+    dict(sum=P, ss=256), dict(r=P, rs=256, sum=P, ss=256), dict(x=P + 8192, r=P, rs=256, sum=P, ss=256), dict(sum=P + 2048, ss=256),
+    dict(xs=600, sum=P + 1024, ss=600), dict(xs=600, r=P + 1024, rs=600, sum=P + 1024, ss=600), dict(rows=1, sum=P + 1024, ss=256)])
+def test_norm_quant_takes_a_sum_in_place_or_beside_its_inputs(bpe, change):
+    assert _norm(bpe, **change) == bpe.EINVAL  # host memory, which is looked at last
+    assert "device memory" in bpe._lib.bpe_last_error().decode()
+
+
 def _product(bpe, **change):
     a = dict(a=P, as_=256, sa=P, sas=2, b=P, bs=256, sb=P, sbs=2, m=4, n=8, k=256, out=P, os=8, kind=0)
     a.update(change)

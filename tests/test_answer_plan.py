@@ -27,6 +27,9 @@ int parts(uint64_t rows, uint64_t group_rows, uint64_t most_groups, uint64_t *ou
 int share_bytes(uint64_t a, uint64_t a_bytes, uint64_t b, uint64_t b_bytes) {
     return bpek::share_bytes((const void*)a, a_bytes, (const void*)b, b_bytes);
 }
+int share_rows(uint64_t a, uint64_t a_stride, uint64_t b, uint64_t b_stride, uint64_t rows, uint64_t width) {
+    return bpek::share_rows((const void*)a, a_stride, (const void*)b, b_stride, rows, width);
+}
 int kernels() { return bpek::PK_COUNT; }
 int first_tile() { return bpek::PK_TILE_128_64; }
 // the kernel of a product and the kind of its pieces
@@ -49,7 +52,7 @@ def plan(tmp_path_factory):
     u64 = ctypes.c_uint64
     lib.groups_in_x.argtypes, lib.groups_in_x.restype, lib.groups_in_y.restype = [u64], u64, u64
     lib.kernel.argtypes = [u64, u64, u64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
-    lib.share_bytes.argtypes = [u64] * 4
+    lib.share_bytes.argtypes, lib.share_rows.argtypes = [u64] * 4, [u64] * 6
     lib.parts.argtypes = [u64, u64, u64, ctypes.POINTER(u64), ctypes.c_int]
     return lib
 
@@ -98,6 +101,18 @@ def test_arrays_that_share_memory(plan):
     for a, n, b, m, want in [(0, 10, 10, 5, 0), (10, 5, 0, 10, 0), (0, 10, 9, 5, 1), (9, 5, 0, 10, 1), (0, 100, 40, 1, 1),
                              (40, 1, 0, 100, 1), (7, 3, 7, 3, 1), (7, 0, 7, 3, 0), (7, 3, 7, 0, 0), (5, 0, 0, 100, 0)]:
         assert plan.share_bytes(0x1000 + a, n, 0x1000 + b, m) == want
+
+
+def test_rows_that_share_memory(plan):
+    """Against the sets of their bytes."""
+    def taken(at, stride, rows, width):
+        return {at + r * stride + i for r in range(rows) for i in range(width)}
+    for rows, stride, width in [(1, 9, 4), (2, 4, 4), (3, 9, 4), (4, 10, 5), (3, 7, 4), (2, 12, 3)]:
+        for off in range(-40, 41):
+            want = bool(taken(100, stride, rows, width) & taken(100 + off, stride, rows, width))
+            assert plan.share_rows(100, stride, 100 + off, stride, rows, width) == want, (rows, stride, width, off)
+    assert plan.share_rows(100, 4, 112, 8, 3, 4) == 0 and plan.share_rows(100, 4, 108, 8, 3, 4) == 1
+    assert plan.share_rows(100, 4, 100, 4, 0, 4) == 0
 
 
 def _kernel(plan, m, n, k, aligned_rows, exact, tiled=True):
